@@ -58,7 +58,7 @@ struct FwdShared {
   static constexpr int Q = Path<E>::kMain, QS = kStride<L, Q>, NS = kStride<L, NP>;
   alignas(16) L bt[NP * QS], br[Q * NS], cr[Q * NS];
   alignas(16) L xt[HB][kPT * QS];
-  alignas(16) L m[HB][Path<E>::kOut][Q * QS];
+  alignas(16) L m[HB][Path<E>::kTerms][Q * QS];
   Decay<Q> dec[HB][2];  // of this chunk and the next
 };
 
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256 * HB, kSides<E>) void scan_kernel(selinv_scan_a
                                                         int npt, const float *init, int total) {
   using S = FwdShared<E, NP, HB>;
   using L = typename S::L;
-  constexpr int Q = S::Q, QS = S::QS, NS = S::NS, NT = NP / 16, MT = Path<E>::kOut, TQ = Q / 16;
+  constexpr int Q = S::Q, QS = S::QS, NS = S::NS, NT = NP / 16, MT = Path<E>::kTerms, TQ = Q / 16;
   constexpr int NTH = 256 * HB;
   __shared__ S sh;
   const int tid = threadIdx.x, lane = tid & 63;

@@ -33,17 +33,17 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kPT = 64;  // rows of the state (elements of x) per workgroup
 
 // L: what the fragments hold; Q: tokens of a chunk; kMain: of the forward main
-// pass's; kOut, kState: terms of a float32 operand whose product ends in a
-// 16-bit output / in a float32 one
+// pass's; kTerms: terms of an operand that was computed in float32; kBack: of
+// those whose product ends in a 16-bit gradient
 template <typename E>
 struct Path {
   using L = float;
-  static constexpr int Q = 32, kMain = 32, kOut = 1, kState = 1;
+  static constexpr int Q = 32, kMain = 32, kTerms = 1, kBack = 1;
 };
 template <>
 struct Path<__bf16> {
   using L = __bf16;
-  static constexpr int Q = 64, kMain = 32, kOut = 2, kState = 3;
+  static constexpr int Q = 64, kMain = 32, kTerms = 3, kBack = 2;
 };
 
 template <typename L>
@@ -357,7 +357,7 @@ __device__ inline void state_update(f32x4 (&st)[NP / 16], const typename Path<E>
                                     const typename Path<E>::L *bt, const float *w, float total,
                                     float sign, int r, int g) {
   using L = typename Path<E>::L;
-  constexpr int N3 = Path<E>::kState;
+  constexpr int N3 = Path<E>::kTerms;
 #pragma unroll
   for (int k = 0; k < NP / 16; ++k) st[k] *= total;
   // Four column tiles at a time, the next four's fragments under way while

@@ -36,7 +36,7 @@ constexpr int kWaves = 8, kThreads = 64 * kWaves;
 template <typename E, int NP>
 struct VjpShared {
   using L = typename Path<E>::L;
-  static constexpr int Q = Path<E>::Q, TQ = Q / 16, MT = Path<E>::kOut;
+  static constexpr int Q = Path<E>::Q, TQ = Q / 16, MT = Path<E>::kBack;
   static constexpr int QS = kStride<L, Q>, NS = kStride<L, NP>, XS = kStride<L, kPT>;
   alignas(16) L br[Q * NS], bt[NP * QS], ct[NP * QS];
   struct Head {
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
   using S = VjpShared<E, NP>;
   using L = typename S::L;
   constexpr int Q = S::Q, TQ = S::TQ, MT = S::MT, QS = S::QS, NS = S::NS, XS = S::XS;
-  constexpr int NT = NP / 16, N3 = Path<E>::kState, KP = kPT / 16;
+  constexpr int NT = NP / 16, N3 = Path<E>::kTerms, KP = kPT / 16;
   constexpr int IS = kWaves / NT;                  // wavefronts that share a column tile n
   constexpr int TI = TQ > IS ? TQ / IS : 1;        // token tiles of each
   constexpr int TX = TQ / 2;                       // token tiles of x_bar per wavefront
