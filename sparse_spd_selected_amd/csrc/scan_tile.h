@@ -33,17 +33,18 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kPT = 64;  // rows of the state (elements of x) per workgroup
 
 // L: what the fragments hold; Q: tokens of a chunk; kMain: of the forward main
-// pass's; kTerms: terms of an operand that was computed in float32; kBack: of
-// those whose product ends in a 16-bit gradient
+// pass's; kTerms: terms of an operand that was computed in float32 (two would
+// be enough for a 16-bit output's size, but round one in a thousand of them the
+// other way)
 template <typename E>
 struct Path {
   using L = float;
-  static constexpr int Q = 32, kMain = 32, kTerms = 1, kBack = 1;
+  static constexpr int Q = 32, kMain = 32, kTerms = 1;
 };
 template <>
 struct Path<__bf16> {
   using L = __bf16;
-  static constexpr int Q = 64, kMain = 32, kTerms = 3, kBack = 2;
+  static constexpr int Q = 64, kMain = 32, kTerms = 3;
 };
 
 template <typename L>
@@ -70,6 +71,20 @@ __device__ inline f32x4 wide(bf16x4 v) {
 template <typename L>
 __device__ inline Frag<L> frag(const L *p) {
   return *reinterpret_cast<const Frag<L> *>(p);
+}
+
+// four neighbours down column r of a 16 x 16 tile that lies by rows, rows 4 g ..
+// + 3: the fragment of the transposed tile
+__device__ inline bf16x4 frag_down(const __bf16 *tile, int stride, int r, int g) {
+  // 16 lanes read four rows of 16 elements, four elements each, and the load hands
+  // every lane its column
+  const __bf16 *p = tile + (4 * g + (r >> 2)) * stride + 4 * (r & 3);
+  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+      (__attribute__((address_space(3))) bf16x4 *)const_cast<__bf16 *>(p));
+}
+__device__ inline f32x4 frag_down(const float *tile, int stride, int r, int g) {
+  const float *p = tile + 4 * g * stride + r;
+  return f32x4{p[0], p[stride], p[2 * stride], p[3 * stride]};
 }
 
 // acc += A B over K = 32: fragments k and k + 16 of either operand

@@ -36,7 +36,7 @@ constexpr int kWaves = 8, kThreads = 64 * kWaves;
 template <typename E, int NP>
 struct VjpShared {
   using L = typename Path<E>::L;
-  static constexpr int Q = Path<E>::Q, TQ = Q / 16, MT = Path<E>::kBack;
+  static constexpr int Q = Path<E>::Q, TQ = Q / 16, MT = Path<E>::kTerms;
   static constexpr int QS = kStride<L, Q>, NS = kStride<L, NP>, XS = kStride<L, kPT>;
   alignas(16) L br[Q * NS], bt[NP * QS], ct[NP * QS];
   struct Head {
@@ -46,8 +46,8 @@ struct VjpShared {
     alignas(16) Head head;
     alignas(16) L cr[Q * NS];  // until the scores are formed
   };
-  // (W L d) by rows i and by columns j, (G L) by columns j
-  alignas(16) L mc[MT][Q * QS], md[MT][Q * QS], me[MT][Q * QS];
+  // (W L d) and (G L) by columns j
+  alignas(16) L md[MT][Q * QS], me[MT][Q * QS];
   // what a head leaves for its sums over the chunk; two heads in turn
   struct Sums {
     float rs[TQ][Q]; // row sums of Z by column tile
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
   using S = VjpShared<E, NP>;
   using L = typename S::L;
   constexpr int Q = S::Q, TQ = S::TQ, MT = S::MT, QS = S::QS, NS = S::NS, XS = S::XS;
-  constexpr int NT = NP / 16, N3 = Path<E>::kTerms, KP = kPT / 16;
+  constexpr int NT = NP / 16, KP = kPT / 16;
   constexpr int IS = kWaves / NT;                  // wavefronts that share a column tile n
   constexpr int TI = TQ > IS ? TQ / IS : 1;        // token tiles of each
   constexpr int TX = TQ / 2;                       // token tiles of x_bar per wavefront
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
     }
   } else {
     // ---- B, C and their scores
-    for (int i = tid; i < 3 * MT * Q * QS; i += kThreads) sh.mc[0][i] = static_cast<L>(0.0f);
+    for (int i = tid; i < 2 * MT * Q * QS; i += kThreads) sh.md[0][i] = static_cast<L>(0.0f);
     {
       Tile<E, Q, NP, kThreads> tb, tc;
       const E *Bm = static_cast<const E *>(a.Bm) + b * a.b_sb + gr * a.b_sg + t0 * a.b_st;
@@ -373,8 +373,6 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
         for (int m = 0; m < MT; ++m) {
           *reinterpret_cast<Frag<L> *>(&sh.md[m][j * QS + ib]) = tw.t[m];
           if (first) *reinterpret_cast<Frag<L> *>(&sh.me[m][j * QS + ib]) = tg.t[m];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sh.mc[m][(ib + e) * QS + j] = tw.t[m][e];
         }
         f32x4 up;  // sums of the column from row ib + e down
         up[3] = zd[3], up[2] = zd[2] + up[3], up[1] = zd[1] + up[2], up[0] = zd[0] + up[1];
@@ -414,9 +412,9 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
         for (int i = 0; i < Q / 16; ++i)
           yt[i] = frag<L>(sh.head.yt + (16 * pw + r) * QS + 16 * i + 4 * g);
         __builtin_amdgcn_sched_barrier(0);
-        Terms<L, N3> rr[NT];
+        Terms<L, MT> rr[NT];
 #pragma unroll
-        for (int k = 0; k < NT; ++k) rr[k] = split<N3>(Sum2<L>::sign(k / 2, r2[k]), L());
+        for (int k = 0; k < NT; ++k) rr[k] = split<MT>(Sum2<L>::sign(k / 2, r2[k]), L());
         float dd = 0.0f;
 #pragma unroll
         for (int k = 0; k < TX; ++k) {
@@ -433,7 +431,7 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
           __builtin_amdgcn_sched_barrier(0);
           Sum2<L> t2;
 #pragma unroll
-          for (int i = N3 - 1; i >= 0; --i)
+          for (int i = MT - 1; i >= 0; --i)
 #pragma unroll
             for (int m = 0; m < NT; m += 2)
               mma(t2.at(m / 2), rr[m].t[i], rr[m + 1].t[i], bm[m], bm[m + 1]);
@@ -484,9 +482,7 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
       }
       if (i0 < TQ) {
         r = fresh(r), g = fresh(g), n = 16 * nt + r;
-        // B_bar is rounded to 16 bits, so R gets two terms here
-        Terms<L, N3> ss[KP];
-        Terms<L, MT> rr[KP];
+        Terms<L, MT> ss[KP], rr[KP];
         // as above: the next token tile's operands are on their way
         Frag<L> nx[KP], ny[KP], bt[Q / 16], ct[Q / 16];
         auto fetch_xy = [&](int i) {
@@ -504,23 +500,26 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < KP; ++k)
-          ss[k] = split<N3>(Sum2<L>::sign(k / 2, sf[k]), L()), rr[k] = split<MT>(rf[k], L());
+          ss[k] = split<MT>(Sum2<L>::sign(k / 2, sf[k]), L()), rr[k] = split<MT>(rf[k], L());
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
           r = fresh(r), g = fresh(g);
           const int it = i0 + i, ib = 16 * it + 4 * g;
-          Frag<L> x[KP], y[KP], mc[MT][Q / 16], md[MT][Q / 16];
+          Frag<L> x[KP], y[KP], mc[2][Q / 16], md[2][Q / 16];
 #pragma unroll
           for (int k = 0; k < KP; ++k) x[k] = nx[k], y[k] = ny[k];
-          // columns j of (W L d) up to the diagonal, and its rows from there on
+          // columns j of (W L d) up to the diagonal, and its rows from there on: a
+          // term, and the next one while it is multiplied
+          auto fetch_w = [&](int m) {
 #pragma unroll
-          for (int j = 0; j < Q / 16; ++j)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const int o = (16 * it + r) * QS + 16 * j + 4 * g;
-              if (j / 2 * 2 <= it) mc[m][j] = frag<L>(&sh.mc[m][o]);
-              if (j / 2 * 2 + 2 > it) md[m][j] = frag<L>(&sh.md[m][o]);
+            for (int j = 0; j < Q / 16; ++j) {
+              if (j / 2 * 2 <= it)
+                mc[m & 1][j] = frag_down(&sh.md[m][16 * j * QS + 16 * it], QS, r, g);
+              if (j / 2 * 2 + 2 > it)
+                md[m & 1][j] = frag<L>(&sh.md[m][(16 * it + r) * QS + 16 * j + 4 * g]);
             }
+          };
+          fetch_w(MT - 1);
           if (i + 1 < TI) fetch_xy(i + 1);
           const f32x4 from = *reinterpret_cast<const f32x4 *>(dec.from + ib);
           const f32x4 weight = *reinterpret_cast<const f32x4 *>(dec.weight + ib);
@@ -529,23 +528,25 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
           Sum2<L> s1;
           f32x4 t3 = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int m = N3 - 1; m >= 0; --m)
+          for (int m = MT - 1; m >= 0; --m)
 #pragma unroll
             for (int k = 0; k < KP; k += 2) {
               mma(s1.at(k / 2), y[k], y[k + 1], ss[k].t[m], ss[k + 1].t[m]);
-              if (m < MT) mma(t3, x[k], x[k + 1], rr[k].t[m], rr[k + 1].t[m]);
+              mma(t3, x[k], x[k + 1], rr[k].t[m], rr[k + 1].t[m]);
             }
           const f32x4 t1 = s1.value() * from;
           add_rows(su.rpart[nt] + ib, first, t1 * cw, r);
           dC[i] += t1;
           dB[i] += t3 * weight;
 #pragma unroll
-          for (int m = MT - 1; m >= 0; --m)
+          for (int m = MT - 1; m >= 0; --m) {
+            if (m > 0) fetch_w(m - 1);
 #pragma unroll
             for (int j = 0; j < Q / 16; j += 2) {
-              if (j <= it) mma(dC[i], mc[m][j], mc[m][j + 1], bt[j], bt[j + 1]);
-              if (j + 2 > it) mma(dB[i], md[m][j], md[m][j + 1], ct[j], ct[j + 1]);
+              if (j <= it) mma(dC[i], mc[m & 1][j], mc[m & 1][j + 1], bt[j], bt[j + 1]);
+              if (j + 2 > it) mma(dB[i], md[m & 1][j], md[m & 1][j + 1], ct[j], ct[j + 1]);
             }
+          }
         }
       }
       __syncthreads();  // done with the head's x, y_bar and scores

@@ -38,3 +38,14 @@ def test_outputs_are_rounded_once(ssa):
     y, _ = ssa.selective_scan(x, dt, A, Bm, Cm, Dv, bias, state=st)
     ry, _ = sr.selective_scan(softplus=True, lengths=None, **ref_inputs(c, None))
     assert moved(y, ry) <= 2.0 ** -12
+
+
+def test_gradients_are_rounded_once(ssa):
+    say("selective_scan_vjp", CASE)
+    c = scan_case(*CASE)
+    x, dt, A, Bm, Cm, Dv, bias, st, _, yb, sob = c
+    got = ssa.selective_scan_vjp(x, dt, A, Bm, Cm, yb, sob, Dv, bias, state=st)
+    ref = sr.grads(lambda **k: sr.selective_scan(softplus=True, lengths=None, **k),
+                   ref_inputs(c, None), (sr.wide(yb), sr.wide(sob)))
+    for g, name in ((got[0], "x"), (got[3], "Bm"), (got[4], "Cm")):
+        assert moved(g, ref[name]) <= 2.0 ** -12, name
