@@ -223,7 +223,7 @@ __global__ __launch_bounds__(256 * HB, kSides<E>) void scan_kernel(selinv_scan_a
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = t0 + i < len ? acc[e] : 0.0f;
       if (V4) {  // rows past T are dropped
-        buffer_store4(buffer_rows(y, row, static_cast<int>(a.T) - t0 - 16 * it), yoff,
+        buffer_store4(buffer_rows(y, row, min(16, static_cast<int>(a.T) - t0 - 16 * it)), yoff,
                       narrow<E, 4>(f));
       } else if (t0 + i < a.T) {
 #pragma unroll

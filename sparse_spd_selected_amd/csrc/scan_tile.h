@@ -177,10 +177,20 @@ __device__ inline void put_cols(L *dst, int stride, int t, int c, const Block<E>
 // rows' bytes by the load itself, which gives zero (and a store that does
 // nothing) past them.  The offset past all of them:
 constexpr unsigned kOutside = 0xffffffffu;
+// The size of a buffer is 32 bits wide, so it holds a chunk's rows and not what
+// is left of an array: at most kBufferRows rows, kBufferStride elements apart at
+// most.
+constexpr int kBufferRows = 64, kBufferStride = 1 << 21;
+constexpr int buffer_bytes(int64_t st, int rows, int size) {
+  return rows <= 0 ? 0
+                   : static_cast<int>((rows < kBufferRows ? rows : kBufferRows) * st * size);
+}
+static_assert(buffer_bytes(kBufferStride, 1 << 30, 4) == int64_t{kBufferRows} * kBufferStride * 4);
+static_assert(buffer_bytes(65536, 32768, 2) == kBufferRows * 65536 * 2, "rows of 2^32 bytes");
 template <typename E>
 __device__ inline __amdgpu_buffer_rsrc_t buffer_rows(const E *p, int64_t st, int rows) {
-  const int bytes = rows > 0 ? rows * static_cast<int>(st) * static_cast<int>(sizeof(E)) : 0;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E *>(p), 0, bytes, 0x00027000);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E *>(p), 0,
+                                           buffer_bytes(st, rows, sizeof(E)), 0x00027000);
 }
 template <typename E>
 __device__ inline typename Vec<E, 4>::Reg buffer_load4(__amdgpu_buffer_rsrc_t rows, unsigned off) {
@@ -487,7 +497,7 @@ hipError_t chain_segments(int64_t heads, int64_t state, const Sweeps &sw, hipStr
 // and token strides that Tile can take (rows that overlap go the other way)
 template <typename E>
 inline bool rows_of_four(const selinv_scan_args &a, bool vjp) {
-  auto near = [](int64_t st, int cols) { return st >= cols && st < (1 << 21); };
+  auto near = [](int64_t st, int cols) { return st >= cols && st < kBufferStride; };
   const bool ok = a.N % 4 == 0 && a.P % 4 == 0 && near(a.x_st, a.P) && near(a.b_st, a.N) &&
                   near(a.c_st, a.N) && (!vjp || near(a.yb_st, a.P)) &&
                   near(static_cast<int64_t>(a.H) * a.P, a.P) &&

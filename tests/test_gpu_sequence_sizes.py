@@ -1,0 +1,44 @@
+"""The sequence operators where a size or an offset passes 32 bits."""
+import pytest
+import torch
+
+from test_gpu_sequence import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ssa():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import sparse_spd_selected_amd as m
+    m.lib()
+    return m
+
+
+def test_a_row_of_four_gib(ssa):
+    """A row's outputs are 2^32 bytes: all of them are written, and the first
+    ones are those of the row's beginning alone."""
+    B, T, H, P, N = 1, 32768, 256, 256, 4
+    say("selective_scan", B, T, H, P, N)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(0)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device=DEV).bfloat16()
+
+    x = normal(B, T, 1, P).expand(B, T, H, P)  # the heads share their input
+    dt, Bm, Cm = normal(B, T, H), normal(B, T, 1, N), normal(B, T, 1, N)
+    A = -torch.rand(H, generator=gen, device=DEV) - 0.5
+    # memory that y is likely to get: an output that is not written shows
+    torch.full((B * T * H * P,), float("nan"), dtype=torch.bfloat16, device=DEV)
+    y, out = ssa.selective_scan(x, dt, A, Bm, Cm)
+    assert y.numel() * y.element_size() == 2 ** 32
+    assert all(torch.isfinite(v).all() for v in y.view(64, -1)) and torch.isfinite(out).all()
+    head, _ = ssa.selective_scan(x[:, :256], dt[:, :256], A, Bm[:, :256], Cm[:, :256])
+    assert torch.equal(y[:, :256], head)
+    # and the last ones those of the end, from the state before it
+    _, st = ssa.selective_scan(x[:, :-256], dt[:, :-256], A, Bm[:, :-256], Cm[:, :-256])
+    tail, last = ssa.selective_scan(x[:, -256:], dt[:, -256:], A, Bm[:, -256:], Cm[:, -256:],
+                                    state=st)
+    assert torch.equal(y[:, -256:], tail) and torch.equal(out, last)
