@@ -56,10 +56,12 @@ class WaitTimeout(SelinvError):
 
 
 def build():
-    """Compile libselinv.so in place (hipcc, gfx950)."""
+    """Compile libselinv.so in place (hipcc, gfx950), and the sequence
+    operators' binding."""
     from . import buildlib as _b
     global _lib
     _lib = None
+    _sequence.release()
     return _b.build()
 
 

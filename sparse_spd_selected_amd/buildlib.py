@@ -94,13 +94,11 @@ def build(verbose: bool = False, out: str = LIB, build_dir: str = BUILD_DIR,
     """Compile every source and link `out`.  `host_flags` go to the host side
     of every compile and to the link (the tests use it for a host-sanitizer
     build of the library in its own build_dir).  The library in its own place
-    is built with its binding."""
+    is built with its binding, whose failure is raised once the library stands."""
     os.makedirs(build_dir, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         binding = ex.submit(build_binding) if out == LIB else None
         objs = list(ex.map(lambda src: _compile(src, build_dir, host_flags), SOURCES))
-        if binding is not None:
-            binding.result()
     tmp = out + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH] + list(host_flags) + \
         ["-o", tmp] + objs
@@ -108,6 +106,8 @@ def build(verbose: bool = False, out: str = LIB, build_dir: str = BUILD_DIR,
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, out)
+    if binding is not None:
+        binding.result()
     if verbose:
         print("built", out)
     return out

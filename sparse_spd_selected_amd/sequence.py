@@ -27,7 +27,7 @@ import torch
 
 _TYPES = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
 MAX_W, MAX_HEAD, MAX_P, MAX_N = 8, 512, 256, 128
-_bound = None  # the compiled binding, once it has the library's addresses
+_bound = None  # the compiled binding, once it has the loaded library's addresses
 
 _i64, _i32, _f32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
 
@@ -57,9 +57,8 @@ ScanArgs = _struct(
 
 
 def declare(L):
-    """Called when the library loads: ctypes signatures of the entry points,
-    and their addresses for the compiled binding."""
-    global _bound
+    """Called when the library loads: ctypes signatures of the entry points."""
+    release()
     sz = ctypes.c_size_t
     for sfx in _TYPES.values():
         for name, args in (("conv", ConvArgs), ("conv_step", ConvArgs), ("qkrot", QkrotArgs),
@@ -78,9 +77,12 @@ def declare(L):
         f = getattr(L, "selinv_%s_workspace_bytes" % name)
         f.argtypes = args
         f.restype = sz
-    from . import _seqbind, _status
-    _seqbind.bind(lambda name: ctypes.cast(getattr(L, name), _vp).value, _raw_stream, _status)
-    _bound = _seqbind
+
+
+def release():
+    """The library goes or is another one: the next call binds anew."""
+    global _bound
+    _bound = None
 
 
 # the stream's handle without a Stream object around it, where torch offers that
@@ -89,10 +91,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 def _binding():
-    """The compiled binding; the library is loaded with the first call."""
-    if _bound is None:
-        from . import lib
-        lib()
+    """The compiled binding.  The first call here loads it, and the library: the
+    rest of the package does without it."""
+    global _bound
+    from . import _status, lib
+    L = lib()
+    try:
+        from . import _seqbind
+    except ImportError as e:
+        raise ImportError("the binding of the sequence operators is not built for this Python and "
+                          "torch (run sparse_spd_selected_amd.build())") from e
+    _seqbind.bind(lambda name: ctypes.cast(getattr(L, name), _vp).value, _raw_stream, _status)
+    _bound = _seqbind
     return _bound
 
 
