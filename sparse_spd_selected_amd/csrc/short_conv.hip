@@ -226,8 +226,11 @@ __global__ __launch_bounds__(256) void conv_vjp_kernel(selinv_conv_args a, int c
         }
       }
     };
-    // `own`: a token of this run; those past it only complete x_bar
+    // `own`: a token of this run; those past it only complete x_bar.  Past the row's
+    // end nothing may come of what the window still holds, which a cotangent of zero
+    // would pass on where it is not finite: chosen, not multiplied away.
     auto token = [&](int k, const Vec<E, V> &x, const Vec<E, V> &y, auto own) {
+      const bool in = t0 + k < len;
       widen(x, win[K - 1]);
       float yv[V], done[V];
       widen(y, yv);
@@ -237,16 +240,20 @@ __global__ __launch_bounds__(256) void conv_vjp_kernel(selinv_conv_args a, int c
 #pragma unroll
         for (int j = 0; j < K; ++j)
           if (used<K>(a, j)) v = fmaf(w[j][i], win[j][i], v);
-        float gi = yv[i];  // zero past the row's length
+        float gi = yv[i];
         if (a.silu) {
           const float sg = sigmoid(v);
           gi *= sg * fmaf(v, 1.0f - sg, 1.0f);
         }
+        if (!in) gi = 0.0f;
         g[K - 1][i] = gi;
         if (own) {
           db[i] += gi;
 #pragma unroll
-          for (int j = 0; j < K; ++j) dw[j][i] = fmaf(gi, win[j][i], dw[j][i]);
+          for (int j = 0; j < K; ++j) {
+            const float sum = fmaf(gi, win[j][i], dw[j][i]);
+            dw[j][i] = in ? sum : dw[j][i];
+          }
         }
         done[i] = 0.0f;
 #pragma unroll
