@@ -451,7 +451,8 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
           const float dj = dec.d[j];
           float f[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = fmaf(dj, acc[e], D * yv[e]);
+          for (int e = 0; e < 4; ++e)  // past the row: chosen, as acc may not be finite
+            f[e] = j < rows ? fmaf(dj, acc[e], D * yv[e]) : 0.0f;
           E *o = xbar + ((tok + 16 * jt) * a.H + h) * a.P + pt;
           if (V4) {  // rows past T are dropped
             buffer_store4(buffer_rows(o, row, all - 16 * jt),
@@ -563,13 +564,14 @@ __global__ __launch_bounds__(kThreads) void vjp_kernel(selinv_scan_args a, const
         const int t = 16 * (i0 + i) + 4 * g + e;
         if (t >= all) continue;
         const int64_t o = ((tok + t) * a.G + gr) * a.N + n;
+        const float db = t < rows ? dB[i][e] : 0.0f, dc = t < rows ? dC[i][e] : 0.0f;
         if (slices == 1) {
-          static_cast<E *>(a.B_bar)[o] = static_cast<E>(dB[i][e]);
-          static_cast<E *>(a.C_bar)[o] = static_cast<E>(dC[i][e]);
+          static_cast<E *>(a.B_bar)[o] = static_cast<E>(db);
+          static_cast<E *>(a.C_bar)[o] = static_cast<E>(dc);
         } else {
           const int64_t size = a.B * a.T * a.G * a.N;
-          bc[2 * slice * size + o] = dB[i][e];
-          bc[(2 * slice + 1) * size + o] = dC[i][e];
+          bc[2 * slice * size + o] = db;
+          bc[(2 * slice + 1) * size + o] = dc;
         }
       }
     }

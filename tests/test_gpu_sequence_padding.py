@@ -52,3 +52,37 @@ def test_short_conv_gradient(ssa, ty, T, C, W, bad, silu):
     assert torch.equal(got[0][1, :T - 5 - W], want[0][1, :T - 5 - W])
     if not silu:  # linear: the inputs' gradients do not depend on the inputs
         assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+
+
+@pytest.mark.parametrize("ty,H,P,G,N", [("bf16", 4, 64, 2, 128), ("bf16", 3, 20, 1, 7),
+                                        ("f32", 2, 64, 1, 32), ("f16", 2, 33, 2, 20)])
+def test_selective_scan_gradient(ssa, ty, H, P, G, N):
+    """States and their cotangents that are not finite spoil their row's tokens
+    alone, not the padding behind them; an empty row's spoil no sum."""
+    say("selective_scan_vjp", ty, H, P, G, N)
+    B, T, lengths = 3, 100, [100, 37, 0]
+    r = sr.rng(P)
+    x, yb = (up(sr.normal(r, B, T, H, P), TYPES[ty]) for _ in range(2))
+    Bm, Cm = (up(sr.normal(r, B, T, G, N), TYPES[ty]) for _ in range(2))
+    dt, st, sob = up(sr.normal(r, B, T, H), TYPES[ty]), up(sr.normal(r, B, H, P, N)), up(
+        sr.normal(r, B, H, P, N))
+    A, D, bias = -up(sr.normal(r, H).abs()) - 0.1, up(sr.normal(r, H)), up(sr.normal(r, H) - 1)
+    ln = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+
+    def vjp(st, sob):
+        return ssa.selective_scan_vjp(x, dt, A, Bm, Cm, yb, sob, D, bias, state=st, lengths=ln)
+
+    want = vjp(st, sob)
+    for bad in (float("nan"), float("inf")):
+        for row in (1, 2):
+            s, o = st.clone(), sob.clone()
+            s[row], o[row] = bad, bad
+            got = vjp(s, o)
+            for k in (0, 1, 3, 4):  # the tokens' gradients: x, dt, B, C
+                for i, n in enumerate(lengths):
+                    assert not got[k][i, n:].any(), (bad, row, k, i)
+                    if i != row:
+                        assert torch.equal(got[k][i], want[k][i])
+            if row == 2:
+                for k in (2, 5, 6):
+                    assert torch.equal(got[k], want[k])
