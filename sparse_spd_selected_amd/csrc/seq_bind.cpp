@@ -89,6 +89,12 @@ Maybe check_slots(const Maybe &slots, int64_t B, int64_t n_slots, const Tensor &
   return plain(slots, "slots", {B}, at::kInt, like);
 }
 
+// a size that the structs hold in 32 bits
+int32_t small(int64_t n, const char *name) {
+  TORCH_CHECK_VALUE(n <= INT32_MAX, name, " must be below 2^31, got ", n);
+  return static_cast<int32_t>(n);
+}
+
 void *ptr(const Tensor &t) { return t.data_ptr(); }
 void *ptr(const Maybe &t) { return t ? t->data_ptr() : nullptr; }
 template <typename T>
@@ -146,9 +152,10 @@ struct Conv {
                       "weight must be [C, W] with 1 <= W <= ", SELINV_CONV_MAX_W);
     B = x.size(0), T = token ? 1 : x.size(1), C = x.size(-1), W = weight_.size(1);
     TORCH_CHECK_VALUE(C >= 1, "x needs at least one channel");
+    a.C = small(C, "the channels");
     weight = plain(weight_, "weight", {C, W}, at::kFloat, x);
     bias = plain(bias_, "bias", {C}, at::kFloat, x);
-    a.B = B, a.T = T, a.C = static_cast<int32_t>(C), a.W = static_cast<int32_t>(W), a.silu = silu;
+    a.B = B, a.T = T, a.W = static_cast<int32_t>(W), a.silu = silu;
     a.x_sb = x.stride(0), a.x_st = token ? 0 : x.stride(1);
     a.x = ptr(x), a.weight = as<float>(weight), a.bias = as<float>(bias);
   }
@@ -208,6 +215,7 @@ struct Qk {
     const int64_t B = q.size(0), T = q.size(1), D = q.size(3);
     TORCH_CHECK_VALUE(q.size(2) >= 1 && D >= 1 && D <= SELINV_QKROT_MAX_D,
                       "need at least one query head and 1 <= D <= ", SELINV_QKROT_MAX_D);
+    a.Hq = small(q.size(2), "the query heads");
     q_weight = plain(qw, "q_weight", {D}, at::kFloat, q);
     if (k_) {
       k = tokens(*k_, "k", q);
@@ -240,11 +248,11 @@ struct Qk {
     }
     a.B = B, a.T = T, a.table_rows = rows;
     a.q_sb = q.stride(0), a.q_st = q.stride(1), a.q_sh = q.stride(2);
-    a.Hq = static_cast<int32_t>(q.size(2)), a.D = static_cast<int32_t>(D);
+    a.D = static_cast<int32_t>(D);
     a.R = static_cast<int32_t>(R), a.interleaved = interleaved, a.eps = static_cast<float>(eps);
     a.q = ptr(q), a.q_weight = as<float>(q_weight);
     if (k && k->size(2)) {
-      a.Hk = static_cast<int32_t>(k->size(2));
+      a.Hk = small(k->size(2), "the key heads");
       a.k_sb = k->stride(0), a.k_st = k->stride(1), a.k_sh = k->stride(2);
       a.k = ptr(k), a.k_weight = as<float>(k_weight);
     }
@@ -308,6 +316,7 @@ struct Scan {
                       "need 1 <= P <= ", SELINV_SCAN_MAX_P, " and 1 <= N <= ", SELINV_SCAN_MAX_N);
     TORCH_CHECK_VALUE(G >= 1 && H >= 1 && H % G == 0,
                       "the heads must be a multiple of the groups (H=", H, ", G=", G, ")");
+    a.H = small(H, "the heads"), a.G = static_cast<int32_t>(G);
     Cm = tokens(Cm_, "Cm", x, Bm.sizes());
     dt = tokens(dt_, "dt", x, x.sizes().slice(0, lead + 1));
     A = plain(A_, "A", {H}, at::kFloat, x);
@@ -319,7 +328,7 @@ struct Scan {
     a.c_sb = Cm.stride(0), a.c_sg = Cm.stride(lead);
     if (!token)
       a.x_st = x.stride(1), a.dt_st = dt.stride(1), a.b_st = Bm.stride(1), a.c_st = Cm.stride(1);
-    a.H = static_cast<int32_t>(H), a.P = static_cast<int32_t>(P), a.G = static_cast<int32_t>(G);
+    a.P = static_cast<int32_t>(P);
     a.N = static_cast<int32_t>(N), a.softplus = softplus;
     a.x = ptr(x), a.dt = ptr(dt), a.Bm = ptr(Bm), a.Cm = ptr(Cm), a.A = as<float>(A);
     a.D = as<float>(D), a.dt_bias = as<float>(dt_bias);

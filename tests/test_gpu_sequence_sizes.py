@@ -42,3 +42,22 @@ def test_a_row_of_four_gib(ssa):
     tail, last = ssa.selective_scan(x[:, -256:], dt[:, -256:], A, Bm[:, -256:], Cm[:, -256:],
                                     state=st)
     assert torch.equal(y[:, -256:], tail) and torch.equal(out, last)
+
+
+def test_sizes_past_32_bits_are_refused(ssa):
+    """Not taken for what their lower halves say.  Without rows nothing is
+    allocated."""
+    def z(*shape, dtype=torch.bfloat16):
+        return torch.zeros(shape, dtype=dtype, device=DEV)
+
+    many, f32 = 2 ** 32 + 8, torch.float32
+    for call in (
+            lambda: ssa.short_conv(z(0, 1, many), z(1, 1, dtype=f32).expand(many, 1)),
+            lambda: ssa.short_conv_step(z(0, many), z(0, 0, many), z(1, 1, dtype=f32).expand(many, 1)),
+            lambda: ssa.qk_norm_rotate(z(0, 1, many, 8), None, z(8, dtype=f32), None),
+            lambda: ssa.qk_norm_rotate(z(0, 1, 1, 8), z(0, 1, many, 8), z(8, dtype=f32),
+                                       z(8, dtype=f32)),
+            lambda: ssa.selective_scan(z(0, 1, many, 4), z(0, 1, many), z(1, dtype=f32).expand(many),
+                                       z(0, 1, 1, 4), z(0, 1, 1, 4))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
