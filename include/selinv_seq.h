@@ -35,9 +35,11 @@
  *   - Outputs must not alias inputs or each other (the _step state excepted).
  *   - An empty batch or length (B = 0, T = 0) is valid: the states and
  *     gradients that exist are written.
- *   - Sizes: B T and B (T + 128) C / 16 below 2^30, B T below 2^26 for
- *     selinv_qkrot_*, B H at most 2^20 and B (T + 128) H / 64 below 2^30 for
- *     selinv_scan_*; larger calls are refused.
+ *   - Sizes: B (T + 128) and B (T + 128) C / 16 at most 2^30, C at most 2^27;
+ *     B T at most 2^26 - 4 for selinv_qkrot_*; B H at most 2^20 and B (T + 128)
+ *     H / 64 at most 2^30 for selinv_scan_*; the chunks of selinv_scan_vjp_*, B
+ *     G times T over 64 (bfloat16) or 32 rounded up, below 2^23.  Larger calls
+ *     are refused.
  *   - Return: SELINV_OK, SELINV_ERR_INVALID_ARG or SELINV_ERR_HIP.
  */
 #ifndef SELINV_SEQ_H

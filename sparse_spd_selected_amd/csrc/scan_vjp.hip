@@ -675,6 +675,12 @@ size_t scan_vjp_workspace_bytes(int dtype_bytes, int64_t B, int64_t T, int32_t H
 }
 
 template <typename E>
+bool scan_vjp_fits(int64_t B, int64_t T, int32_t G) {
+  // below 2^32 threads; there are slices only where there are less than 256 of these
+  return B * chunks_of(T, Path<E>::Q) * G < (int64_t(1) << 32) / kThreads;
+}
+
+template <typename E>
 hipError_t scan_vjp_launch(const selinv_scan_args &a, void *ws, hipStream_t s) {
   const Plan p(a.B, a.T, a.H, a.P, a.G, a.N, Path<E>::Q, ws);
   hipError_t e = hipSuccess;
@@ -713,6 +719,7 @@ hipError_t scan_vjp_launch(const selinv_scan_args &a, void *ws, hipStream_t s) {
 }
 
 #define SELINV_SCAN_VJP_INSTANCE(E) \
+  template bool scan_vjp_fits<E>(int64_t, int64_t, int32_t); \
   template hipError_t scan_vjp_launch<E>(const selinv_scan_args &, void *, hipStream_t);
 SELINV_SCAN_VJP_INSTANCE(float)
 SELINV_SCAN_VJP_INSTANCE(_Float16)

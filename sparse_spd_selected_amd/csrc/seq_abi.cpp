@@ -8,8 +8,9 @@
 namespace {
 
 // Bounds that keep every product of sizes below 2^63 and every launch below
-// 2^32 threads.
+// 2^32 threads (the scan's gradient has one of its own, by the chunks).
 constexpr int64_t kTokens = int64_t(1) << 30;
+constexpr int32_t kChannels = 1 << 27;
 inline bool bad_batch(int64_t B, int64_t T, int64_t most = kTokens) {
   return B < 0 || T < 0 || B >= most || T >= most || (B > 0 && T + 128 > kTokens / B) ||
          (T > 0 && B >= (most + T - 1) / T);
@@ -26,7 +27,7 @@ inline int status(hipError_t e) { return e == hipSuccess ? SELINV_OK : SELINV_ER
 
 // ------------------------------------------------------ short convolution
 inline bool bad_conv(const selinv_conv_args &a) {
-  return bad_batch(a.B, a.T) || a.C < 1 || a.W < 1 || a.W > SELINV_CONV_MAX_W ||
+  return bad_batch(a.B, a.T) || a.C < 1 || a.C > kChannels || a.W < 1 || a.W > SELINV_CONV_MAX_W ||
          // a thread per four tokens and channel at worst
          (a.B > 0 && a.T + 128 > kTokens * 16 / a.B / a.C);
 }
@@ -70,7 +71,7 @@ int conv_vjp_entry(const selinv_conv_args *p, void *ws, size_t ws_bytes, void *s
 }
 
 // ------------------------------------------------- head norm and rotation
-constexpr int64_t kQkTokens = int64_t(1) << 26;  // a wavefront each
+constexpr int64_t kQkTokens = (int64_t(1) << 26) - 3;  // below this: a wavefront each
 constexpr int32_t kHeads = 1 << 16;
 inline bool bad_qkrot(const selinv_qkrot_args &a) {
   if (bad_batch(a.B, a.T, kQkTokens) || a.Hq < 1 || a.Hk < 0 || a.Hq > kHeads || a.Hk > kHeads ||
@@ -152,6 +153,7 @@ template <typename E>
 int scan_vjp_entry(const selinv_scan_args *p, void *ws, size_t ws_bytes, void *stream) {
   if (!p || bad_scan(*p) || skewed_scan<E>(*p)) return SELINV_ERR_INVALID_ARG;
   const selinv_scan_args &a = *p;
+  if (!selinv::scan_vjp_fits<E>(a.B, a.T, a.G)) return SELINV_ERR_INVALID_ARG;
   if (!a.A_bar) return SELINV_ERR_INVALID_ARG;
   if (a.B * a.T > 0 && (!a.y_bar || !a.x_bar || !a.dt_bar || !a.B_bar || !a.C_bar))
     return SELINV_ERR_INVALID_ARG;
