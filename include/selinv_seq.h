@@ -203,8 +203,13 @@ SELINV_API int selinv_scan_bf16(const selinv_scan_args *a, void *workspace,
 SELINV_API int selinv_scan_step_f32(const selinv_scan_args *a, void *stream);
 SELINV_API int selinv_scan_step_f16(const selinv_scan_args *a, void *stream);
 SELINV_API int selinv_scan_step_bf16(const selinv_scan_args *a, void *stream);
+/* Two float32 states a head and chunk of 32 tokens, which is enough for every
+ * type of dtype_bytes; the chunks of bfloat16 are of 64, and its calls need no
+ * more than the second query says. */
 SELINV_API size_t selinv_scan_vjp_workspace_bytes(int dtype_bytes, int64_t B, int64_t T, int32_t H,
                                                   int32_t P, int32_t G, int32_t N);
+SELINV_API size_t selinv_scan_vjp_bf16_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t P,
+                                                       int32_t G, int32_t N);
 SELINV_API int selinv_scan_vjp_f32(const selinv_scan_args *a, void *workspace,
                                    size_t workspace_bytes, void *stream);
 SELINV_API int selinv_scan_vjp_f16(const selinv_scan_args *a, void *workspace,

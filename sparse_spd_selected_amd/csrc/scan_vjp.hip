@@ -665,13 +665,9 @@ struct Plan {
 
 using namespace scan;
 
-size_t scan_vjp_workspace_bytes(int dtype_bytes, int64_t B, int64_t T, int32_t H, int32_t P,
-                                int32_t G, int32_t N) {
-  // float16 shares its size with bfloat16, whose chunks are longer
-  const size_t n32 = Plan(B, T, H, P, G, N, 32, nullptr).bytes;
-  if (dtype_bytes == 4) return n32;
-  const size_t n64 = Plan(B, T, H, P, G, N, 64, nullptr).bytes;
-  return n32 > n64 ? n32 : n64;
+template <typename E>
+size_t scan_vjp_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N) {
+  return Plan(B, T, H, P, G, N, Path<E>::Q, nullptr).bytes;
 }
 
 template <typename E>
@@ -720,6 +716,7 @@ hipError_t scan_vjp_launch(const selinv_scan_args &a, void *ws, hipStream_t s) {
 
 #define SELINV_SCAN_VJP_INSTANCE(E) \
   template bool scan_vjp_fits<E>(int64_t, int64_t, int32_t); \
+  template size_t scan_vjp_workspace_bytes<E>(int64_t, int64_t, int32_t, int32_t, int32_t, int32_t); \
   template hipError_t scan_vjp_launch<E>(const selinv_scan_args &, void *, hipStream_t);
 SELINV_SCAN_VJP_INSTANCE(float)
 SELINV_SCAN_VJP_INSTANCE(_Float16)

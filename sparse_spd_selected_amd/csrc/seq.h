@@ -33,8 +33,8 @@ template <typename E>
 hipError_t scan_launch(const selinv_scan_args &a, void *ws, hipStream_t s);
 template <typename E>
 hipError_t scan_step_launch(const selinv_scan_args &a, hipStream_t s);
-size_t scan_vjp_workspace_bytes(int dtype_bytes, int64_t B, int64_t T, int32_t H, int32_t P,
-                                int32_t G, int32_t N);
+template <typename E>
+size_t scan_vjp_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N);
 // whether the gradient's workgroups, one a chunk and group, fit a launch
 template <typename E>
 bool scan_vjp_fits(int64_t B, int64_t T, int32_t G);

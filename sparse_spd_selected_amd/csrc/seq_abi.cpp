@@ -161,8 +161,8 @@ int scan_vjp_entry(const selinv_scan_args *p, void *ws, size_t ws_bytes, void *s
       skewed<E>(a.C_bar) || skewed<float>(a.state_out_bar) || skewed<float>(a.A_bar) ||
       skewed<float>(a.D_bar) || skewed<float>(a.dt_bias_bar) || skewed<float>(a.state_bar))
     return SELINV_ERR_INVALID_ARG;
-  if (bad_workspace(ws, ws_bytes, selinv::scan_vjp_workspace_bytes(sizeof(E), a.B, a.T, a.H, a.P,
-                                                                   a.G, a.N)))
+  if (bad_workspace(ws, ws_bytes,
+                    selinv::scan_vjp_workspace_bytes<E>(a.B, a.T, a.H, a.P, a.G, a.N)))
     return SELINV_ERR_INVALID_ARG;
   return status(selinv::scan_vjp_launch<E>(a, ws, static_cast<hipStream_t>(stream)));
 }
@@ -187,9 +187,17 @@ size_t selinv_scan_workspace_bytes(int dtype_bytes, int64_t B, int64_t T, int32_
 }
 size_t selinv_scan_vjp_workspace_bytes(int dtype_bytes, int64_t B, int64_t T, int32_t H, int32_t P,
                                        int32_t G, int32_t N) {
+  if (bad_scan_sizes(B, T, H, P, G, N)) return 0;
+  if (dtype_bytes == 4) return selinv::scan_vjp_workspace_bytes<float>(B, T, H, P, G, N);
+  const size_t f16 = selinv::scan_vjp_workspace_bytes<_Float16>(B, T, H, P, G, N);
+  const size_t bf16 = selinv::scan_vjp_workspace_bytes<__bf16>(B, T, H, P, G, N);
+  return f16 > bf16 ? f16 : bf16;
+}
+size_t selinv_scan_vjp_bf16_workspace_bytes(int64_t B, int64_t T, int32_t H, int32_t P, int32_t G,
+                                            int32_t N) {
   return bad_scan_sizes(B, T, H, P, G, N)
              ? 0
-             : selinv::scan_vjp_workspace_bytes(dtype_bytes, B, T, H, P, G, N);
+             : selinv::scan_vjp_workspace_bytes<__bf16>(B, T, H, P, G, N);
 }
 
 size_t selinv_conv_vjp_workspace_bytes(int64_t B, int64_t T, int32_t C, int32_t W) {

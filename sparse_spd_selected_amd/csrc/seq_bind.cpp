@@ -29,6 +29,7 @@ decltype(&selinv_conv_vjp_workspace_bytes) g_conv_vjp_bytes = nullptr;
 decltype(&selinv_qkrot_vjp_workspace_bytes) g_qkrot_vjp_bytes = nullptr;
 decltype(&selinv_scan_workspace_bytes) g_scan_bytes = nullptr;
 decltype(&selinv_scan_vjp_workspace_bytes) g_scan_vjp_bytes = nullptr;
+decltype(&selinv_scan_vjp_bf16_workspace_bytes) g_scan_vjp_bf16_bytes = nullptr;
 PyObject *g_stream = nullptr;  // device index -> handle of its current stream
 PyObject *g_failed = nullptr;  // (status, name): raises
 
@@ -380,9 +381,11 @@ py::tuple selective_scan_vjp(const Tensor &x, const Tensor &dt, const Tensor &A,
   c.a.x_bar = ptr(xb), c.a.dt_bar = ptr(dtb), c.a.B_bar = ptr(Bb), c.a.C_bar = ptr(Cb);
   c.a.A_bar = as<float>(Ab), c.a.D_bar = as<float>(Db), c.a.dt_bias_bar = as<float>(bb);
   c.a.state_bar = as<float>(sb);
-  call(kScanVjp, c.a, c.x,
-       g_scan_vjp_bytes(static_cast<int>(c.x.element_size()), c.a.B, c.a.T, c.a.H,
-                                       c.a.P, c.a.G, c.a.N));
+  const auto &a = c.a;
+  call(kScanVjp, a, c.x,
+       c.x.scalar_type() == at::kBFloat16
+           ? g_scan_vjp_bf16_bytes(a.B, a.T, a.H, a.P, a.G, a.N)
+           : g_scan_vjp_bytes(static_cast<int>(c.x.element_size()), a.B, a.T, a.H, a.P, a.G, a.N));
   return py::make_tuple(xb, dtb, Ab, Bb, Cb, Db, bb, sb);
 }
 
@@ -401,6 +404,7 @@ void bind(const std::function<uintptr_t(const std::string &)> &address, const py
   set(g_qkrot_vjp_bytes, "selinv_qkrot_vjp_workspace_bytes");
   set(g_scan_bytes, "selinv_scan_workspace_bytes");
   set(g_scan_vjp_bytes, "selinv_scan_vjp_workspace_bytes");
+  set(g_scan_vjp_bf16_bytes, "selinv_scan_vjp_bf16_workspace_bytes");
   Py_XDECREF(g_stream);
   Py_XDECREF(g_failed);
   g_stream = stream.inc_ref().ptr();

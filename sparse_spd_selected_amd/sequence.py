@@ -73,7 +73,8 @@ def declare(L):
             f.restype = ctypes.c_int
     for name, args in (("conv_vjp", [_i64, _i64, _i32, _i32]), ("qkrot_vjp", [_i64, _i64, _i32]),
                        ("scan", [ctypes.c_int, _i64, _i64, _i32, _i32, _i32]),
-                       ("scan_vjp", [ctypes.c_int, _i64, _i64, _i32, _i32, _i32, _i32])):
+                       ("scan_vjp", [ctypes.c_int, _i64, _i64, _i32, _i32, _i32, _i32]),
+                       ("scan_vjp_bf16", [_i64, _i64, _i32, _i32, _i32, _i32])):
         f = getattr(L, "selinv_%s_workspace_bytes" % name)
         f.argtypes = args
         f.restype = sz
@@ -189,7 +190,7 @@ def selective_scan_vjp(x, dt, A, Bm, Cm, y_bar, state_out_bar=None, D=None, dt_b
     """Cotangents of (x, dt, A, Bm, Cm, D, dt_bias, state) for a loss of
     selective_scan's outputs: y_bar [B, T, H, P], state_out_bar [B, H, P, N]
     float32 (None = 0).  The forward is recomputed; the workspace holds two
-    float32 states per head and chunk of tokens.  D's, dt_bias's and state's
+    float32 states per head and chunk of 32 tokens (bfloat16: 64).  D's, dt_bias's and state's
     are None where those are."""
     return (_bound or _binding()).selective_scan_vjp(x, dt, A, Bm, Cm, y_bar, state_out_bar, D,
                                                      dt_bias, softplus, state, lengths)

@@ -61,3 +61,22 @@ def test_sizes_past_32_bits_are_refused(ssa):
                                        z(0, 1, 1, 4), z(0, 1, 1, 4))):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def test_scan_gradient_takes_what_it_needs(ssa):
+    """bfloat16: two states a head and chunk of 64 tokens, the outputs, and the
+    sums of the heads and of the shared B and C."""
+    B, T, H, P, G, N = 2, 4096, 16, 64, 1, 128
+    x, yb = (torch.ones(B, T, H, P, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    Bm = torch.ones(B, T, G, N, dtype=torch.bfloat16, device=DEV)
+    dt = torch.zeros(B, T, H, dtype=torch.bfloat16, device=DEV)
+    A = -torch.ones(H, device=DEV)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    got = ssa.selective_scan_vjp(x, dt, A, Bm, Bm, yb)
+    peak = torch.cuda.max_memory_allocated() - before
+    states = 2 * B * H * (T // 64) * P * N * 4
+    outputs = sum(g.numel() * g.element_size() for g in got if g is not None)
+    # beside the states, an eighth of them each for the segments and for the slices of B and C
+    assert peak <= 1.5 * states + outputs, (peak, states, outputs)
