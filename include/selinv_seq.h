@@ -17,14 +17,15 @@
  *   - The suffix names the element type of the token arrays: _f32, _f16,
  *     _bf16.  Parameters (weights, biases, A, D, dt_bias, rotation tables),
  *     their gradients and the scan's states are always float32.  Sums, norms
- *     and states are held in float32 or more; an output is rounded to its type
- *     once.
+ *     and states are held in float32 or more, and enter the scan's products
+ *     with 24 bits at least; an output is rounded to its type once.
  *   - The arguments are passed in a struct; a pointer marked "opt" may be
  *     NULL.  Strides are in elements, the innermost dimension is contiguous;
  *     an array without stride fields is contiguous.  Any alignment of the
  *     element type is accepted; 16-byte aligned rows are the fast case.
  *   - `lengths` (opt, int32 [B]): row r holds lengths[r] tokens (clamped to
- *     0..T) of the padded T.  What lies past them is not read; outputs and
+ *     0..T) of the padded T.  What lies past them has no effect (of the scan's
+ *     dt it may be read and dropped, all else is not read); outputs and
  *     gradients there are written as zero, and the state handed on is the one
  *     after the last token (the initial state for a row of length zero).
  *   - `slots` (opt, int32 [B], the _step calls): row r uses state

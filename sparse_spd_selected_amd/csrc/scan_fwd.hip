@@ -10,12 +10,13 @@
 // kernel chains the segments, and the main pass starts each from its state.
 //
 // Measured for 8192 tokens of 32 heads of 64 x 128 in bfloat16, 32 segments: first
-// pass 26 us, chain 14 (64 MB, 4.6 TB/s), main pass 52; 83 us a call, 130 TFLOP/s
-// of the recurrence's count.  In the main pass a SIMD issues vector instructions
-// 43 % of the time and matrix products 19 %, LDS is busy 30 %: the steps of a
-// chunk wait for each other, and the decays, the splits into bfloat16 terms and
-// the moves into LDS cost more than the products.  Main chunks of 64 tokens with
-// one workgroup a CU took 15 % longer.
+// pass 26 us, chain 14 (64 MB, 4.6 TB/s), main pass 59, each under the profiler; 88
+// us a call where calls follow each other, 121 TFLOP/s of the recurrence's count.
+// In the main pass a SIMD issues vector instructions 45 % of the time and matrix
+// products 21 %, LDS is busy 29 %: the steps of a chunk wait for each other, and the
+// decays, the splits into bfloat16 terms and the moves into LDS cost more than the
+// products.  With two terms of states and scores instead of three it is 6 % shorter;
+// with main chunks of 64 tokens and one workgroup a CU 13 % longer.
 #include <type_traits>
 
 #include "scan_tile.h"
@@ -412,7 +413,7 @@ __global__ __launch_bounds__(256) void chain_kernel(int64_t state, int tiles, in
   }
 }
 
-// Two heads a workgroup where a group's heads pair up (one: 5 % more time for a
+// Two heads a workgroup where a group's heads pair up (one: 7 % more time for a
 // prompt of 8192 tokens and 32 heads).
 inline int heads_together(const selinv_scan_args &a) { return a.H / a.G % 2 ? 1 : 2; }
 
@@ -446,14 +447,18 @@ void run_cut(const selinv_scan_args &a, const Sweeps &sw, hipStream_t s) {
 
 }  // namespace
 
-// 1024 workgroups of one head (512 of two) run at once.  Below half of that the
-// work is cut.  Sweeps without y first share the columns of a state of 128, which
+// In bfloat16 1024 workgroups of one head (512 of two) run at once.  Below half of
+// that the work is cut.  Sweeps without y first share the columns of a state of 128, which
 // reads x twice but has no pass to join them (the gradient's two sweeps at
 // 4 x 4096 x 32 heads: 150 us, against 215 in four segments; in four parts of 32
 // columns 200).  Then rows are cut, into segments of four chunks at least (one or
 // two gain nothing for a prompt of 8192 tokens, eight are slower).  The first pass
 // costs half of the forward's main one, but all of a sweep's, where two segments
 // gain nothing (gradient of 3 x 301 tokens in float32: 55 us in two, 47 in one).
+// The other types' larger fragments let half as many run where N is 128; the same
+// numbers hold for them, as halves lose more at one end than they gain at the other
+// (float32, 64 x 128, this rule or half: 4 x 4096 tokens of 48 heads 562 us or 671,
+// 1 x 8192 of 32 204 or 187).
 int segments_for(int64_t B, int32_t H, int32_t P, int32_t N, int chunks, bool *cut) {
   int64_t wgs = B * H * ((P + kPT - 1) / kPT);
   if (cut) {

@@ -14,8 +14,9 @@
 // alike.  Two such fragments make one K = 32 step.
 //
 // Types.  bfloat16 inputs go into v_mfma_f32_16x16x32_bf16 as they are; an
-// operand that was computed in float32 is written as a sum of bfloat16 terms
-// (8 bits each: two terms leave 2^-17, three 2^-25), one instruction per term.
+// operand that was computed in float32 is written as a sum of three bfloat16
+// terms (8 bits each: they leave 2^-25 of it, two would leave 2^-17), one
+// instruction per term.
 // float32 and float16 inputs use v_mfma_f32_16x16x4_f32 on float32 fragments.
 #pragma once
 
@@ -33,9 +34,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kPT = 64;  // rows of the state (elements of x) per workgroup
 
 // L: what the fragments hold; Q: tokens of a chunk; kMain: of the forward main
-// pass's; kTerms: terms of an operand that was computed in float32 (two would
-// be enough for a 16-bit output's size, but round one in a thousand of them the
-// other way)
+// pass's; kTerms: terms of an operand that was computed in float32 (two round one
+// 16-bit output in a thousand another way than float32 does)
 template <typename E>
 struct Path {
   using L = float;
@@ -306,8 +306,8 @@ __device__ inline float step_of(const selinv_scan_args &a, float v, bool in) {
 }
 
 // dt of the chunk's tokens from t0, lane = token, as it comes: a conversion would
-// wait for the load, and with it for every load before.  Past the row or the
-// chunk: any of the row's values.
+// wait for the load, and with it for every load before.  Past the row's length or
+// the chunk: any of the array's values, which step_of drops.
 template <typename E, int Q>
 __device__ inline E raw_step(const selinv_scan_args &a, const E *dt, int t0, int lane) {
   return dt[max(0, min(t0 + min(lane, Q - 1), static_cast<int>(a.T) - 1)) * a.dt_st];

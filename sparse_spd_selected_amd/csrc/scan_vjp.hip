@@ -20,11 +20,15 @@
 // takes the group's heads in turn: B, C and G are formed once, and B_bar and
 // C_bar are summed over the heads in registers, in a fixed order.
 //
-// Measured for 4 x 4096 tokens of 32 heads of 64 x 128 in 2 groups, bfloat16: 450
-// us a call.  Sweeps 150 us: 537 MB of states written, 3.6 TB/s.  This kernel 300
-// us: the states read back, 700 MB with the operands, 2.3 TB/s; a SIMD issues
-// vector instructions 37 % of the time and matrix products 15 %, LDS is busy 30 %.
-// LDS holds one workgroup a CU, so what waits at its three barriers a head waits.
+// Measured for 4 x 4096 tokens of 32 heads of 64 x 128 in 2 groups, bfloat16: 478
+// us a call where calls follow each other; under the profiler the sweeps take 173
+// us (537 MB of states written) and this kernel 366 (the states read back, 700 MB
+// with the operands); a SIMD issues vector instructions 40 % of the time and matrix
+// products 17 %, LDS is busy 32 %.  LDS holds one workgroup a CU, so what waits at
+// its three barriers a head waits.  (W L d) is kept by columns alone, its rows come
+// by transposing reads: the copy by rows would not fit beside three terms (146 KB
+// of LDS as it is), and two terms, 5 % shorter, round one 16-bit gradient in five
+// hundred the other way.
 #include "scan_tile.h"
 
 namespace selinv {
@@ -639,7 +643,7 @@ struct Plan {
     // One workgroup fits a CU.  The heads of a group are split, at the price
     // of writing and reading B_bar and C_bar once more per slice, until every
     // CU has one (32 heads of 64 x 128, bfloat16: 1 x 1024 tokens in one group
-    // 276 us whole, 69 in sixteen; 4 x 4096 in two groups 451 and 914).
+    // 300 us whole, 69 in sixteen; 4 x 4096 in two groups 466 whole, 506 in two).
     slices = 1;
     while (slices * 2 <= H / G && B * chunks * G * slices < 256) slices *= 2;
     size_t off = 0;

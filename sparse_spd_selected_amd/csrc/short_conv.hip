@@ -9,8 +9,8 @@
 // a run come out of the cache.
 //
 // Measured in 16 bits, four taps (a large copy reaches 5.1 TB/s): forwards over
-// 6 x 1531 tokens of 2304 channels 22 us, 3.9 TB/s; reverse mode of 8 x 2048
-// tokens of 4352 channels 94 us and 5 for the parameters' sums, 4.3 TB/s; a token
+// 6 x 1531 tokens of 2304 channels 21.5 us, 3.9 TB/s; reverse mode of 8 x 2048
+// tokens of 4352 channels 99 us with the parameters' sums, 4.3 TB/s; a token
 // of 2304 channels 4 us, a launch.
 #include <type_traits>
 
@@ -168,12 +168,12 @@ __global__ __launch_bounds__(256) void conv_step_kernel(selinv_conv_args a, unsi
 //   weight_bar[j] = sum g[t] whole[t + j],  bias_bar = sum g[t]
 // with v recomputed from x.  A wavefront's lanes own 64 channel vectors, a
 // workgroup four runs of RUN tokens; the W - 1 tokens of g past a run are
-// recomputed from cached inputs (runs of 16 or 64 tokens: 118 us and 115 where
-// these take 113).  Parameter sums of a workgroup's tokens go to
+// recomputed from cached inputs.  Parameter sums of a workgroup's tokens go to
 // the workspace, [tile][K + 1][C], and are added up in tile order.
 //
 // A run is a chain of steps, so small calls get short ones: eight tokens below
-// 2^23 elements, else 32 (four taps, 16 bits: 300 tokens of 2304 channels 10 us
+// 2^23 elements, else 32 (of 8 x 2048 tokens of 4352 channels runs of 16, 32 and 64
+// take 109 us, 104 and 105, in float32 with 2304 channels 100, 102 and 115; four taps, 16 bits: 300 tokens of 2304 channels 10 us
 // with eight, 19 with 32; 2000 tokens 17 and 20; 4096 23 and 24; 8192 36 and 31).
 inline int run_for(int64_t B, int64_t T, int32_t C) { return B * T * C < 1 << 23 ? 8 : 32; }
 

@@ -15,9 +15,12 @@ sequence (``_step``), which updates a pool of states in place.
 Token arrays are float32, float16 or bfloat16 and may be views (slices of a
 fused projection) whose last dimension is contiguous; parameters are float32.
 ``lengths`` (int32, one per row) marks the tokens of a padded batch: outputs
-and gradients past them are zero, and what stands there is not read.
+and gradients past them are zero, and what stands there has no effect.
 ``slots`` (int32) names the state of each row in the pool; rows with a slot
 outside the pool (-1: idle) get zeros and touch no state.
+
+Like the package's other calls these record nothing for autograd: the gradients
+are the ``_vjp`` calls (``examples/sequence_mixer.py`` wraps them as functions).
 """
 from __future__ import annotations
 
